@@ -275,6 +275,10 @@ paged_append_kernel(const PagedAppendArgs a, int units, int tokens) {
 //    sequences keep all warps busy.
 //  * Two warps prepare the query views (rotation, scale, split into hi and lo, laid out as
 //    fragments) a few ahead, so that the fetch of a pair's queries delays nobody.
+//  * Each tile's product P V is a fresh sum that is added to the warp's total with rounding: the
+//    tensor core cuts what it adds to an accumulator towards zero, so a total kept in its
+//    accumulator lost 1.0e-4 of the result at 131,000 keys a pair and 1.2e-5 at 16,000 (values of
+//    one sign); this way 9e-8, and no slower (128 windowed sequences 120 us, 123 before).
 //  * Rows of a tile that the token does not see (past its end, between sinks and window) are
 //    masked in S and zeroed in the V tile: whatever an unwritten page holds meets no product.
 //    Pages that hold no visible key are not looked up; TMA fills their rows with zeros.
@@ -746,9 +750,9 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
     uint32_t e = 0, joins = 0;
     for (; p.o < n_mine; p.next(a, n_mine)) {
       float m_run = -INFINITY, l_run = 0.f;
-      float oacc[DN][4];
+      float oacc[DN][2];
 #pragma unroll
-      for (int n = 0; n < DN; ++n) oacc[n][0] = oacc[n][1] = oacc[n][2] = oacc[n][3] = 0.f;
+      for (int n = 0; n < DN; ++n) oacc[n][0] = oacc[n][1] = 0.f;
       // tiles o .. o + take - 1 of the run; this warp's are those with index = w modulo PD_WARPS
       int i = (w - p.o) & (PD_WARPS - 1);
       const bool mine = i < p.take;
@@ -824,30 +828,35 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
             ps += pw[nt][0] + pw[nt][1];
           }
           l_run = l_run * alpha + ps;               // this thread's columns; summed per row at the end
-          if (__any_sync(0xFFFFFFFFu, alpha != 1.f)) {
+          uint32_t pa[2][4];
 #pragma unroll
-            for (int n = 0; n < DN; ++n)
-#pragma unroll
-              for (int c = 0; c < 4; ++c) oacc[n][c] *= alpha;
-          }
-#pragma unroll
-          for (int ks = 0; ks < 2; ++ks) {
-            uint32_t pa[4];
+          for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
               const float p0 = pw[2 * ks + hf][0], p1 = pw[2 * ks + hf][1];
               const uint32_t hi = pack_f16x2(p0, p1);
               const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-              pa[2 * hf] = hi;
-              pa[2 * hf + 1] = pack_f16x2(p0 - back.x, p1 - back.y);
+              pa[ks][2 * hf] = hi;
+              pa[ks][2 * hf + 1] = pack_f16x2(p0 - back.x, p1 - back.y);
             }
+          // a fresh product of the tile, added to the sum of the earlier ones with rounding
 #pragma unroll
-            for (int dp = 0; dp < DN / 2; ++dp) {
+          for (int dp = 0; dp < DN / 2; ++dp) {
+            float t[2][4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) t[0][c] = t[1][c] = 0.f;
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
               uint32_t bf[4];
               ldsm_x4_t(vb + ks * part + chunk(8 * (j4 & 1) + r8, 2 * dp + (j4 >> 1)), bf);
-              mma_16816(oacc[2 * dp], pa, bf[0], bf[1]);
-              mma_16816(oacc[2 * dp + 1], pa, bf[2], bf[3]);
+              mma_16816(t[0], pa[ks], bf[0], bf[1]);
+              mma_16816(t[1], pa[ks], bf[2], bf[3]);
             }
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+              for (int c = 0; c < 2; ++c)
+                oacc[2 * dp + n][c] = fmaf(oacc[2 * dp + n][c], alpha, t[n][c] + t[n][c + 2]);
           }
           // every lane's reads (and zeroes) of the stage are done: hand it back to the copies
           __syncwarp();
@@ -864,7 +873,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
 #pragma unroll
       for (int n = 0; n < DN; ++n)
         *reinterpret_cast<float2*>(&sm.o[w][gid][8 * n + 2 * tig]) =
-            make_float2(oacc[n][0] + oacc[n][2], oacc[n][1] + oacc[n][3]);
+            make_float2(oacc[n][0], oacc[n][1]);
       if (tig == 0) { sm.m[w][gid] = m_run; sm.l[w][gid] = lt; }
       const int n_parts = min(p.take, PD_WARPS);
       __threadfence_block();

@@ -1,0 +1,98 @@
+"""What the paged calls promise beside their results: a table's own width, malformed token
+offsets, memory and streams, lengths beyond the table, sums that keep their precision."""
+import numpy as np
+import pytest
+import torch
+
+from long_context_prefill_dca_b200 import q1m
+from long_context_prefill_dca_b200.layer import PagedCache
+from oracle import dca_vs as O
+from tests import paged_reference as R
+
+pytestmark = pytest.mark.gpu
+
+DTYPE = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+# ---- sums over many keys --------------------------------------------------------------------
+# Values of one sign, so that what an accumulator loses adds up. The bound, relative to the result:
+# a key tile's products are 2 to 16 dependent accumulation steps, each of which cuts at most 2^-23 of
+# the sum so far: 2^-20 in the mean. The n / 32 tile sums (weights, and weights times values) are
+# rounded to nearest: n / 32 <= 1,024 steps of a partial sum, sqrt(1024 / 3) 2^-24 rms = 1.1e-6. The
+# weights' errors (2^-22 and 2^-21 S 2^-22 ...) average out over the keys, as their sign is the key's
+# own. 2^-20 + 1.1e-6 = 2.1e-6: 2^-18.8. One accumulator for all keys is cut in one direction at
+# every step: 1e-4 of the result at 131,000 keys of a pair, 1.2e-5 at 16,000 (measured).
+SUM_BOUND = 2.0 ** -18.8
+
+
+def one_signed(w, n, page, seed, extra=0):
+    g = torch.Generator().manual_seed(seed)
+    n_pages = -(-n // page)
+    k = torch.randn(n_pages + extra, w.n_kv_heads, page, w.head_dim, generator=g).half()
+    v = (0.5 + torch.rand(n_pages + extra, w.n_kv_heads, page, w.head_dim, generator=g)).half()
+    rows = lambda t: t[:n_pages].permute(0, 2, 1, 3).reshape(n_pages * page, w.n_kv_heads, w.head_dim)[:n]  # noqa: E731
+    return k, v, rows(k), rows(v), g
+
+
+def assert_unbiased(got, ref):
+    rel = (got.double().cpu().numpy() - ref) / ref
+    assert abs(rel.mean()) <= SUM_BOUND, rel.mean()
+    assert np.sqrt((rel ** 2).mean()) <= SUM_BOUND, np.sqrt((rel ** 2).mean())
+    return rel
+
+
+@pytest.mark.parametrize("w,n", [(R.G8, 131_000), (R.G3_D64, 70_001)], ids=["g8-d128", "g3-d64"])
+def test_decode_f32_sums_of_whole_pairs(w, n):
+    """More (sequence, KV head) pairs than SMs: a pair's keys stay in one CTA, 1/8 of them in one
+    warp's accumulator. All sequences are the same pages."""
+    batch, page = 330 // w.n_kv_heads, 128
+    k, v, kr, vr, g = one_signed(w, n, page, 5)
+    table = torch.arange(k.shape[0], dtype=torch.int32).expand(batch, -1).contiguous()
+    cache = PagedCache(w, k.cuda(), v.cuda(), table.cuda(), "f32")
+    q = (0.3 * torch.randn(batch, w.n_q_heads, w.head_dim, generator=g)).to(DTYPE[w.in_dtype])
+    out = cache.decode(q.cuda(), i32([n] * batch))
+    torch.cuda.synchronize()
+    q1m.check_status()
+    for b in (0, batch // 2, batch - 1):
+        ref, _ = R.attend(w, q[b:b + 1], [n - 1], kr, vr)
+        assert_unbiased(out[b:b + 1], ref)
+
+
+def test_prefill_f32_sums_of_whole_row_tiles():
+    w, n, new, page = R.G8, 18_000, 2_400, 64
+    k, v, kr, vr, g = one_signed(w, n, page, 6)
+    table = torch.arange(k.shape[0], dtype=torch.int32).view(1, -1)
+    cache = PagedCache(w, k.cuda(), v.cuda(), table.cuda(), "f32")
+    q = (0.3 * torch.randn(new, w.n_q_heads, w.head_dim, generator=g)).to(DTYPE[w.in_dtype])
+    out = cache.prefill(q.cuda(), i32([n]), i32([0, new]))
+    torch.cuda.synchronize()
+    q1m.check_status()
+    for r in (0, 7, 1_201, new - 1):
+        ref, _ = R.attend(w, q[r:r + 1], [n - new + r], kr, vr)
+        assert_unbiased(out[r:r + 1], ref)
+
+
+def test_shared_prefix_f32_sums_of_the_largest_batch():
+    """Q1M_MAX_PAGED_BATCH sequences behind a shared prefix, a few keys of their own each."""
+    w, prefix, page, batch = R.G8, 18_048, 64, q1m.MAX_PAGED_BATCH
+    k, v, kr, vr, g = one_signed(w, prefix, page, 7, extra=batch)
+    shared = prefix // page
+    table = torch.full((batch, shared + 1), -1, dtype=torch.int32)
+    table[:, shared] = shared + torch.arange(batch)
+    pre = torch.arange(shared, dtype=torch.int32).cuda()
+    cache = PagedCache(w, k.cuda(), v.cuda(), table.cuda(), "f32")
+    q = (0.3 * torch.randn(batch, w.n_q_heads, w.head_dim, generator=g)).to(DTYPE[w.in_dtype])
+    lens = [prefix + 1 + b % page for b in range(batch)]
+    out = cache.decode_shared(q.cuda(), i32(lens), pre, prefix)
+    torch.cuda.synchronize()
+    q1m.check_status()
+    for b in (0, 777, batch - 1):
+        m = lens[b] - prefix
+        kk = torch.cat([kr, k[shared + b, :, :m].transpose(0, 1)])
+        vv = torch.cat([vr, v[shared + b, :, :m].transpose(0, 1)])
+        ref, _ = R.attend(w, q[b:b + 1], [lens[b] - 1], kk, vv)
+        assert_unbiased(out[b:b + 1], ref)
