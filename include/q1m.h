@@ -355,7 +355,9 @@ q1m_status q1m_dca_decode(const void* q, const void* k, const void* v, int64_t p
  * contiguous cache's (q1m_rope_dca_keys).
  *  - k_pages, v_pages: device [n_pages][n_kv_heads][page_size][head_dim] fp16, 16-byte aligned,
  *    n_pages * n_kv_heads * page_size < 2^31.
- *  - page_table: device int32 [batch][table_stride]. Only entries of pages that hold a visible
+ *  - page_table: device int32, rows of table_width entries that start table_stride entries apart
+ *    (table_width 0: table_stride of them), so the table may be a slice of a larger one: what lies
+ *    between rows and behind the last is never read. Only entries of pages that hold a visible
  *    (attention) or a new (append) position are read; others may be anything, so pages that a
  *    sliding window has left can be given back. A needed entry that is missing or not in
  *    [0, n_pages) latches Q1M_ERR_PAGE; the append then skips that token and the attention
@@ -371,6 +373,7 @@ typedef struct {
   int32_t page_size;
   int32_t n_kv_heads;
   int32_t head_dim;
+  int32_t table_width;
 } q1m_paged_cache;
 
 /* In all calls of this group:

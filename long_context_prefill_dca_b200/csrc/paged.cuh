@@ -20,8 +20,9 @@ constexpr int32_t PG_MAX_LEN = 1 << 30;   // positions of a sequence
 
 // What every paged kernel knows of the cache.
 struct PagedCacheArgs {
-  const int32_t* page_table;   // [batch][table_stride]
-  int64_t table_stride;
+  const int32_t* page_table;   // [batch] rows
+  int64_t table_stride;        // entries between rows
+  int64_t table_width;         // entries of a row: those behind it are not the cache's
   int32_t n_pages;
   int32_t page_log2;           // page_size = 1 << page_log2, 16 .. 128
   int32_t hkv;
@@ -66,7 +67,7 @@ __device__ __forceinline__ bool pg_wait(uint64_t* bar, uint32_t parity, volatile
 // Page of entry `i` of a table row: Q1M_ERR_PAGE is latched and -1 returned when the row has no
 // such entry or the entry is not a page of the cache.
 __device__ __forceinline__ int32_t pg_page(const PagedCacheArgs& c, const int32_t* row, int64_t i) {
-  if (i < c.table_stride) {
+  if (i < c.table_width) {
     const int32_t page = __ldg(row + i);
     if (page >= 0 && page < c.n_pages) return page;
   }

@@ -34,6 +34,9 @@ q1m_status check_heads(int batch, int hq, int hkv, int d) {
   return Q1M_OK;
 }
 
+// Entries of a table row.
+int64_t table_width(const q1m_paged_cache* c) { return c->table_width > 0 ? c->table_width : c->table_stride; }
+
 q1m_status check_cache(const q1m_paged_cache* c, int batch, int hq, const q1m_params* p, const float* table) {
   if (!c) return fail(Q1M_ERR_INVALID, "cache is NULL");
   Q1M_TRY(check_heads(batch, hq, c->n_kv_heads, c->head_dim));
@@ -47,12 +50,14 @@ q1m_status check_cache(const q1m_paged_cache* c, int batch, int hq, const q1m_pa
   if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
     return fail(Q1M_ERR_UNSUPPORTED, "page_size %d (16, 32, 64 or 128 supported)", c->page_size);
   if (c->n_pages <= 0 || c->table_stride <= 0) return fail(Q1M_ERR_INVALID, "n_pages and table_stride must be positive");
+  if (c->table_width < 0 || c->table_width > c->table_stride)
+    return fail(Q1M_ERR_INVALID, "table_width %d is not in 0 .. table_stride", c->table_width);
   if (c->n_pages >= (int64_t)1 << 31 || c->n_pages * c->n_kv_heads * c->page_size >= (int64_t)1 << 31)
     return fail(Q1M_ERR_UNSUPPORTED, "n_pages * n_kv_heads * page_size too large");
   // the tiles of 32 keys of all sequences are counted in 32 bits
   const int64_t most = (int64_t)1 << 30;
-  const int64_t keys = c->table_stride < most / c->page_size ? c->table_stride * c->page_size : most;
-  if (batch * keys >= (int64_t)1 << 35) return fail(Q1M_ERR_UNSUPPORTED, "batch * table_stride * page_size too large");
+  const int64_t width = table_width(c), keys = width < most / c->page_size ? width * c->page_size : most;
+  if (batch * keys >= (int64_t)1 << 35) return fail(Q1M_ERR_UNSUPPORTED, "batch * table_width * page_size too large");
   if ((reinterpret_cast<uintptr_t>(c->k_pages) | reinterpret_cast<uintptr_t>(c->v_pages) | reinterpret_cast<uintptr_t>(table)) & 15)
     return fail(Q1M_ERR_INVALID, "pages and table must be 16-byte aligned");
   return Q1M_OK;
@@ -85,10 +90,11 @@ PagedCacheArgs cache_args(const q1m_paged_cache* c) {
   PagedCacheArgs a{};
   a.page_table = c->page_table;
   a.table_stride = c->table_stride;
+  a.table_width = table_width(c);
   a.n_pages = (int32_t)c->n_pages;
   a.page_log2 = c->page_size == 16 ? 4 : c->page_size == 32 ? 5 : c->page_size == 64 ? 6 : 7;
   a.hkv = c->n_kv_heads;
-  const int64_t held = c->table_stride < PG_MAX_LEN ? c->table_stride * c->page_size : PG_MAX_LEN;
+  const int64_t held = a.table_width < PG_MAX_LEN ? a.table_width * c->page_size : PG_MAX_LEN;
   a.max_len = (int32_t)(held < PG_MAX_LEN ? held : PG_MAX_LEN);
   return a;
 }
@@ -246,7 +252,7 @@ q1m_status paged_decode(const void* q, int64_t q_stride, const int32_t* seq_len,
     PagedAttnArgs t{};
     t.c = a.c;
     t.c.page_table = prefix_table;
-    t.c.table_stride = prefix_len / c->page_size;
+    t.c.table_stride = t.c.table_width = prefix_len / c->page_size;
     t.q = q; t.q_stride = q_stride; t.n_tokens = batch;
     t.q_f32 = p->in_dtype == Q1M_F32;
     t.seq_len = seq_len;

@@ -159,8 +159,9 @@ class PagedCache:
 
     w: the layer (a Workload, or any object with its fields); w.seq_len is not used.
     k_pages, v_pages: float16 [n_pages, Hkv, page_size, D], page_size 16, 32, 64 or 128.
-    page_table: int32 [batch, pages]: position j of sequence b is row j % page_size of page
-    page_table[b, j // page_size]. Only entries of pages a call needs are read.
+    page_table: int32 [batch, pages], a slice of a larger table if need be: position j of sequence
+    b is row j % page_size of page page_table[b, j // page_size]. Only entries of pages a call
+    needs are read.
     table: the RoPE table [dca_chunk, D / 2, 2] when the caller has one already.
 
     A call serves the first len(seq_len) rows of the page table. seq_len (int32, on the device)
@@ -205,9 +206,12 @@ class PagedCache:
             self._bad("set_page_table", "page_table must be int32 [batch, pages] with contiguous rows, on the cache's device")
         if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
             self._bad("set_page_table", "page_table rows must not overlap")
+        if t.shape[1] >= 1 << 31:
+            self._bad("set_page_table", "page_table is too wide")
         self.page_table, self.places = t, t.shape[0]
         self.desc.page_table = t.data_ptr()
         self.desc.table_stride = t.stride(0) if t.shape[0] > 1 else t.shape[1]
+        self.desc.table_width = t.shape[1]
 
     def append(self, k, v, seq_len, cu_tokens=None, stream=None):
         """Writes the new tokens' keys (rotated) and values [tokens, Hkv, D] into their pages:

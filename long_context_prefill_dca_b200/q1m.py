@@ -38,7 +38,7 @@ class PagedCacheDesc(ctypes.Structure):
     """q1m_paged_cache."""
     _fields_ = [("k_pages", c_vp), ("v_pages", c_vp), ("page_table", c_vp), ("n_pages", c_i64),
                 ("table_stride", c_i64), ("page_size", c_i32), ("n_kv_heads", c_i32),
-                ("head_dim", c_i32)]
+                ("head_dim", c_i32), ("table_width", c_i32)]
 
 
 class Q1MError(RuntimeError):

@@ -18,6 +18,51 @@ def i32(x):
     return torch.tensor(x, dtype=torch.int32, device="cuda")
 
 
+def test_a_sliced_table_ends_at_its_own_width():
+    """A table that is a slice of a larger one: the parent's entries beside it (here all valid pages)
+    are not the sequence's. A length or a new position behind the slice latches the page fault in
+    every call, no page outside the slice changes, and the other sequence is right."""
+    w, page, width = R.G2, 32, 6
+    lens = [page * width, 150]
+    c = R.Case(w, lens, page, 7, prefix=128)
+    spare = 100
+    g = torch.Generator().manual_seed(1)
+    more = torch.randn(spare, w.n_kv_heads, page, w.head_dim, generator=g).half()
+    k, v = torch.cat([c.k, more]).cuda(), torch.cat([c.v, more]).cuda()
+    big = (c.n_pages + torch.arange(4 * 20) % spare).view(4, 20).int()
+    own = c.table[:, :width]
+    big[1:3, 4:4 + width] = torch.where((own >= 0) & (own < c.n_pages), own, c.n_pages)
+    big = big.cuda()
+    cache = PagedCache(w, k, v, big[1:3, 4:4 + width], "f32")
+    inside = torch.unique(big[1:3, 4:4 + width]).cpu()
+    outside = torch.ones(c.n_pages + spare, dtype=torch.bool)
+    outside[inside.long()] = False
+    before = k.cpu().view(torch.int16).clone(), v.cpu().view(torch.int16).clone()
+    q = c.queries(2)
+    ref, _ = R.attend(w, q[1:], [149], c.kc[1], c.vc[1])
+    tol, _ = R.bounds(w, q[1:], c.kc[1], c.vc[1], False)
+    qd, pre = q.cuda(), c.prefix_table.cuda()
+    for over in (1, page, 5 * page):
+        ln = i32([lens[0] + over, 150])
+        for call in (lambda: cache.decode(qd, ln), lambda: cache.prefill(qd, ln, i32([0, 1, 2])),
+                     lambda: cache.decode_shared(qd, ln, pre, 128)):
+            out = call()
+            assert q1m.status_poll() == -8 and q1m.status_poll() == 0
+            R.check(w, out[1:], None, ref, None, tol, 0, False)
+    x = torch.randn(2, w.n_kv_heads, w.head_dim, generator=g).bfloat16().cuda()
+    for over in (1, page, 5 * page):
+        cache.append(x, x, i32([lens[0] + over, 150]))
+        assert q1m.status_poll() == -8 and q1m.status_poll() == 0
+    assert torch.equal(v[int(big[2, 4 + 149 // page]), :, 149 % page], x[1].half())
+    for now, old in zip((k, v), before):
+        assert torch.equal(now.cpu().view(torch.int16)[outside], old[outside])
+        same = now.cpu().view(torch.int16) == old
+        assert int((~same).any(-1).any(-1).any(-1).sum()) == 1     # sequence 1's page alone
+    cache.decode(qd, i32(lens))
+    cache.append(x, x, i32(lens))
+    assert q1m.status_poll() == 0
+
+
 # ---- sums over many keys --------------------------------------------------------------------
 # Values of one sign, so that what an accumulator loses adds up. The bound, relative to the result:
 # a key tile's products are 2 to 16 dependent accumulation steps, each of which cuts at most 2^-23 of
