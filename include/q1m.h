@@ -379,7 +379,8 @@ typedef struct {
 /* In all calls of this group:
  *  - cu_tokens (device int32 [batch + 1], cu_tokens[0] = 0, non-decreasing, at most n_tokens)
  *    gives sequence b the call's rows cu_tokens[b] .. cu_tokens[b + 1] - 1; rows behind
- *    cu_tokens[batch] are neither read nor written.
+ *    cu_tokens[batch] are neither read nor written. A malformed cu_tokens latches Q1M_ERR_INVALID
+ *    and the call writes nothing.
  *  - seq_len (device int32 [batch]) is each sequence's length with the call's tokens, which
  *    are its last ones. A length of 0 marks an unused place of the batch (its rows may hold
  *    anything). One beyond what a table row holds latches Q1M_ERR_PAGE.
@@ -438,8 +439,7 @@ size_t q1m_paged_prefill_scratch_bytes(int64_t n_tokens, int batch, int n_q_head
 
 /* Attention of a ragged batch of prompts (or prompt chunks): query row cu_tokens[b] + r of
  * sequence b with n rows sits at position seq_len[b] - n + r, and the keys up to there are in
- * the cache already. Any number of Q heads per KV head. A malformed cu_tokens latches
- * Q1M_ERR_INVALID and writes nothing. */
+ * the cache already. Any number of Q heads per KV head. */
 q1m_status q1m_paged_prefill(const void* q, int64_t q_stride, int64_t n_tokens,
                              const int32_t* cu_tokens, const int32_t* seq_len, int batch,
                              int64_t window, int64_t sinks, const q1m_paged_cache* cache,

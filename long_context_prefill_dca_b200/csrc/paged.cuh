@@ -64,15 +64,19 @@ __device__ __forceinline__ bool pg_wait(uint64_t* bar, uint32_t parity, volatile
   return __all_sync(0xFFFFFFFFu, ok);
 }
 
-// Page of entry `i` of a table row: Q1M_ERR_PAGE is latched and -1 returned when the row has no
-// such entry or the entry is not a page of the cache.
+// Page of entry `i` of a table row, -1 when the row has no such entry or the entry is not a page of
+// the cache.
+__device__ __forceinline__ int32_t pg_entry(const PagedCacheArgs& c, const int32_t* row, int64_t i) {
+  if (i >= c.table_width) return -1;
+  const int32_t page = __ldg(row + i);
+  return page < c.n_pages ? page : -1;
+}
+
+// The same of a needed page: Q1M_ERR_PAGE is latched when there is none.
 __device__ __forceinline__ int32_t pg_page(const PagedCacheArgs& c, const int32_t* row, int64_t i) {
-  if (i < c.table_width) {
-    const int32_t page = __ldg(row + i);
-    if (page >= 0 && page < c.n_pages) return page;
-  }
-  latch(Q1M_ERR_PAGE);
-  return -1;
+  const int32_t page = pg_entry(c, row, i);
+  if (page < 0) latch(Q1M_ERR_PAGE);
+  return page;
 }
 
 // Length of a sequence. One that its table row cannot hold is cut (Q1M_ERR_PAGE is latched):
@@ -182,6 +186,12 @@ paged_append_kernel(const PagedAppendArgs a, int units, int tokens) {
     const int tl = threadIdx.x / units, u = threadIdx.x - tl * units, g = u / n8;
     ahead.load_kv(a, t0 + tl, g * a.d + (u - g * n8) * 8);
   }
+  // cu may be anything: every block looks all of it over before the first store
+  bool malformed = false, missing = false;
+  if (a.cu != nullptr) {
+    malformed = threadIdx.x == 0 && (__ldg(a.cu) != 0 || __ldg(a.cu + a.batch) > a.n_tokens);
+    for (int b = threadIdx.x; b < a.batch; b += PG_APPEND_THREADS) malformed |= __ldg(a.cu + b + 1) < __ldg(a.cu + b);
+  }
   // the block's tokens, up to 32 a warp
   const int per_warp = (tokens + PG_APPEND_THREADS / 32 - 1) / (PG_APPEND_THREADS / 32);
   {
@@ -202,8 +212,9 @@ paged_append_kernel(const PagedAppendArgs a, int units, int tokens) {
       if (a.cu == nullptr) p = (int64_t)__ldg(a.seq_len + b) - 1;
       else if (b < a.batch) p = (int64_t)__ldg(a.seq_len + b) - ((int64_t)__ldg(a.cu + b + 1) - (t0 + i));
       if (p >= 0) {
-        const int32_t page = pg_page(a.c, a.c.page_table + b * a.c.table_stride, p >> a.c.page_log2);
+        const int32_t page = pg_entry(a.c, a.c.page_table + b * a.c.table_stride, p >> a.c.page_log2);
         const int64_t in_page = p & ((1 << a.c.page_log2) - 1);
+        missing = page < 0;
         if (page >= 0) dst = (((int64_t)page * a.c.hkv) << a.c.page_log2) + in_page;
         pos = (int32_t)(p % a.L);
       }
@@ -211,7 +222,11 @@ paged_append_kernel(const PagedAppendArgs a, int units, int tokens) {
       pos_of[i] = pos;
     }
   }
-  __syncthreads();
+  if (__syncthreads_or(malformed)) {
+    if (threadIdx.x == 0) latch(Q1M_ERR_INVALID);
+    return;
+  }
+  if (missing) latch(Q1M_ERR_PAGE);
   bool bad = false;
   int it = threadIdx.x;
   if (it < items) {

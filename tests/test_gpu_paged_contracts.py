@@ -63,6 +63,29 @@ def test_a_sliced_table_ends_at_its_own_width():
     assert q1m.status_poll() == 0
 
 
+@pytest.mark.parametrize("batch,cu", [
+    (2, [0, 30, 61]), (2, [1, 30, 60]), (2, [0, 40, 30]), (2, [0, -5, 60]), (2, [30, 30, 60]),
+    (300, [0] * 299 + [60, 50]), (300, [0, 60] + [55] + [60] * 298), (1, [0, 1 << 30]), (1, [-7, 60]),
+], ids=lambda x: None)
+def test_append_rejects_malformed_token_offsets(batch, cu):
+    """Nothing is written, whichever entry is wrong (every table entry is a valid page here)."""
+    w, page = R.G2, 16
+    n_pages = 8 * batch
+    k = torch.full((n_pages, w.n_kv_heads, page, w.head_dim), 3.0, dtype=torch.float16, device="cuda")
+    v = k.clone()
+    table = torch.arange(n_pages, dtype=torch.int32, device="cuda").view(batch, 8)
+    cache = PagedCache(w, k, v, table, "f32")
+    x = torch.randn(60, w.n_kv_heads, w.head_dim, device="cuda").bfloat16()
+    cache.append(x, x, i32([60] * batch), i32(cu))
+    assert q1m.status_poll() == -1 and q1m.status_poll() == 0
+    assert (k == 3).all() and (v == 3).all()
+    good = [0] * batch + [60]
+    cache.append(x, x, i32([60] * batch), i32(good))
+    assert q1m.status_poll() == 0
+    at = table[-1].long()
+    assert torch.equal(v[at].transpose(1, 2).reshape(128, w.n_kv_heads, w.head_dim)[:60], x.half())
+
+
 # ---- sums over many keys --------------------------------------------------------------------
 # Values of one sign, so that what an accumulator loses adds up. The bound, relative to the result:
 # a key tile's products are 2 to 16 dependent accumulation steps, each of which cuts at most 2^-23 of
