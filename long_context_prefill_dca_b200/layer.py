@@ -162,7 +162,8 @@ class PagedCache:
     page_table: int32 [batch, pages], a slice of a larger table if need be: position j of sequence
     b is row j % page_size of page page_table[b, j // page_size]. Only entries of pages a call
     needs are read.
-    table: the RoPE table [dca_chunk, D / 2, 2] when the caller has one already.
+    table: the RoPE table [dca_chunk, D / 2, 2] when the caller has one already; otherwise the
+    constructor computes it and waits until it is there.
 
     A call serves the first len(seq_len) rows of the page table. seq_len (int32, on the device)
     holds each sequence's length with the call's tokens, which are its last; cu_tokens (int32
@@ -194,6 +195,8 @@ class PagedCache:
             with self._on("__init__", None):
                 table = torch.empty(w.dca_chunk, self.d // 2, 2, dtype=torch.float32, device=self.device)
                 q1m.rope_table(table, w.dca_chunk, self.d, w.rope_base)
+                if not torch.cuda.is_current_stream_capturing():
+                    torch.cuda.current_stream().synchronize()   # the first call may come on any stream
         elif (table.dtype != torch.float32 or table.numel() < w.dca_chunk * self.d or not table.is_contiguous()
               or table.device != self.device):
             self._bad("__init__", "table must be contiguous float32 [dca_chunk, head_dim / 2, 2], on the cache's device")

@@ -86,6 +86,31 @@ def test_append_rejects_malformed_token_offsets(batch, cu):
     assert torch.equal(v[at].transpose(1, 2).reshape(128, w.n_kv_heads, w.head_dim)[:60], x.half())
 
 
+def test_a_new_cache_can_be_used_on_any_stream_at_once():
+    """The angles that the constructor computes are there for the first call, whatever stream that
+    uses and whatever was queued before them."""
+    w = R.G2
+    c = R.Case(w, [300], 16, 2)
+    g = torch.Generator().manual_seed(3)
+    x = torch.randn(300, w.n_kv_heads, w.head_dim, generator=g).bfloat16().cuda()
+    ln, cu, table = i32([300]), i32([0, 300]), c.table.cuda()
+    want = PagedCache(w, c.k.cuda(), c.v.cuda(), table)
+    want.append(x, x, ln, cu)
+    k, v = c.k.cuda(), c.v.cuda()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    stale = torch.zeros_like(want.table)              # what the new table's memory holds before
+    del stale
+    torch.cuda._sleep(200_000_000)
+    cache = PagedCache(w, k, v, table)
+    cache.append(x, x, ln, cu, stream=side)
+    torch.cuda.synchronize()
+    q1m.check_status()
+    at = c.table[0, :19].long()
+    assert torch.equal(k[at, :, :4].view(torch.int16), want.k_pages[at, :, :4].view(torch.int16))
+    assert torch.equal(k.view(torch.int16), want.k_pages.view(torch.int16))
+
+
 # ---- sums over many keys --------------------------------------------------------------------
 # Values of one sign, so that what an accumulator loses adds up. The bound, relative to the result:
 # a key tile's products are 2 to 16 dependent accumulation steps, each of which cuts at most 2^-23 of
