@@ -170,7 +170,9 @@ class PagedCache:
     [batch + 1]) the rows of ragged batches. q, k and v may be slices of a fused projection
     (any token stride that is a multiple of 8). Calls queue their work on `stream` (a
     torch.cuda.Stream; default: the current stream of the cache's device) and can be captured;
-    outputs and scratch come from PyTorch's allocator on that stream. Device-side faults (a
+    outputs and scratch come from PyTorch's allocator on that stream. A call with stream= marks its
+    tensors as used there, and its result as used on the caller's current stream, so both may be
+    dropped at once; ordering the streams is the caller's (wait_stream). Device-side faults (a
     missing page, fp16 overflow) are reported by q1m.check_status()."""
 
     def __init__(self, w, k_pages, v_pages, page_table, out_dtype: str = "f32", table=None):
@@ -220,8 +222,8 @@ class PagedCache:
         """Writes the new tokens' keys (rotated) and values [tokens, Hkv, D] into their pages:
         one token per sequence, or the ragged batch of cu_tokens."""
         if stream is not None or torch.cuda.current_device() != self.index:
-            with self._on("append", stream):
-                return self.append(k, v, seq_len, cu_tokens)
+            return self._elsewhere("append", stream, lambda: self.append(k, v, seq_len, cu_tokens),
+                                   k, v, seq_len, cu_tokens)
         n, batch = k.shape[0], self._batch("append", seq_len, cu_tokens)
         if v.shape[0] != n:
             self._bad("append", "k and v must have the same number of tokens")
@@ -233,8 +235,8 @@ class PagedCache:
         over all its keys or, with a window, the last `window` and the first `sinks`.
         Returns out [batch, Hq, D]; lse (optional) is [Hq, batch]."""
         if stream is not None or torch.cuda.current_device() != self.index:
-            with self._on("decode", stream):
-                return self.decode(q, seq_len, window, sinks, out, lse)
+            return self._elsewhere("decode", stream, lambda: self.decode(q, seq_len, window, sinks, out, lse),
+                                   q, seq_len, out, lse)
         batch = self._batch("decode", seq_len, None)
         qs = self._rows("decode", "q", q, self.hq, batch)
         out = self._outputs("decode", q, out, lse)
@@ -247,8 +249,8 @@ class PagedCache:
         """decode() over all keys when the first prefix_len positions of every sequence are the
         pages prefix_table (int32): they are read once for the whole batch."""
         if stream is not None or torch.cuda.current_device() != self.index:
-            with self._on("decode_shared", stream):
-                return self.decode_shared(q, seq_len, prefix_table, prefix_len, out, lse)
+            return self._elsewhere("decode_shared", stream, lambda: self.decode_shared(q, seq_len, prefix_table, prefix_len, out, lse),
+                                   q, seq_len, prefix_table, out, lse)
         batch = self._batch("decode_shared", seq_len, None)
         qs = self._rows("decode_shared", "q", q, self.hq, batch)
         self._ints("decode_shared", "prefix_table", prefix_table)
@@ -264,8 +266,8 @@ class PagedCache:
         """Causal attention of a ragged batch of prompts (or prompt chunks) q [tokens, Hq, D] over
         the cache, which holds their keys already. Rows behind cu_tokens[batch] are not written."""
         if stream is not None or torch.cuda.current_device() != self.index:
-            with self._on("prefill", stream):
-                return self.prefill(q, seq_len, cu_tokens, window, sinks, out, lse)
+            return self._elsewhere("prefill", stream, lambda: self.prefill(q, seq_len, cu_tokens, window, sinks, out, lse),
+                                   q, seq_len, cu_tokens, out, lse)
         batch = self._batch("prefill", seq_len, cu_tokens)
         qs, n = self._rows("prefill", "q", q, self.hq), q.shape[0]
         out = self._outputs("prefill", q, out, lse)
@@ -320,6 +322,21 @@ class PagedCache:
 
     def _stream(self):
         return torch._C._cuda_getCurrentRawStream(self.index)
+
+    def _elsewhere(self, call, stream, run, *tensors):
+        """run() with the cache's device, and the stream a call is given, current. The memory of what
+        that stream reads and writes is kept until it is done, the result's until the caller's is."""
+        caller = torch.cuda.current_stream(self.device)
+        with self._on(call, stream):
+            out = run()
+            if stream is None or stream == caller or torch.cuda.is_current_stream_capturing():
+                return out
+            for t in (*tensors, self.k_pages, self.v_pages, self.page_table, self.table):
+                if t is not None:
+                    t.record_stream(stream)
+        if out is not None:
+            out.record_stream(caller)
+        return out
 
     @contextmanager
     def _on(self, call, stream):

@@ -111,6 +111,88 @@ def test_a_new_cache_can_be_used_on_any_stream_at_once():
     assert torch.equal(k.view(torch.int16), want.k_pages.view(torch.int16))
 
 
+def delayed(stream):
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(400_000_000)
+
+
+def reuse(t, value):
+    """Memory of t's size and type, taken again and again, with `value` in it."""
+    return [torch.full_like(t, value) for _ in range(4)]
+
+
+def test_inputs_may_be_dropped_once_a_call_on_another_stream_is_queued():
+    """Keys, values, queries, lengths, offsets and a replaced page table whose last reference goes
+    while the work still waits on `stream`."""
+    w = R.G2
+    lens, new = [300, 40], [200, 40]
+    c = R.Case(w, lens, 16, 2)
+    g = torch.Generator().manual_seed(3)
+    x0 = torch.randn(240, w.n_kv_heads, w.head_dim, generator=g).bfloat16().cuda()
+    q0 = c.queries(240).cuda()
+    table = c.table.clone()
+    table[(table < 0) | (table >= c.n_pages)] = 0
+    want = PagedCache(w, c.k.cuda(), c.v.cuda(), table.cuda())
+    want.append(x0, x0, i32(lens), i32([0, 200, 240]))
+    want_p = want.prefill(q0, i32(lens), i32([0, 200, 240]))
+    want_d = want.decode(q0[:2], i32(lens))
+    cache = PagedCache(w, c.k.cuda(), c.v.cuda(), table.cuda())
+    side = torch.cuda.Stream()
+    for t in (x0, q0, i32(lens)):                     # kernels are loaded before anything waits
+        reuse(t, 1), t.clone()
+    torch.cuda.synchronize()
+    delayed(side)
+    x, q, q2, ln, cu = x0.clone(), q0.clone(), q0[:2].clone(), i32(lens), i32([0, 200, 240])
+    torch.cuda.current_stream().synchronize()         # the copies are there; the side stream still sleeps
+    cache.append(x, x, ln, cu, stream=side)
+    got_p = cache.prefill(q, ln, cu, stream=side)
+    got_d = cache.decode(q2, ln, stream=side)
+    cache.set_page_table(torch.zeros_like(cache.page_table))
+    junk = []
+    del x
+    junk += reuse(x0, 7.0)
+    del q
+    junk += reuse(q0, 7.0)
+    del q2
+    junk += reuse(q0[:2].clone(), 7.0)
+    del ln, cu
+    junk += reuse(i32(lens), 1) + reuse(i32([0, 200, 240]), 0)
+    junk += reuse(cache.page_table, 1)
+    torch.cuda.synchronize()
+    q1m.check_status()
+    assert torch.equal(cache.k_pages.view(torch.int16), want.k_pages.view(torch.int16))
+    assert torch.equal(cache.v_pages.view(torch.int16), want.v_pages.view(torch.int16))
+    assert torch.equal(got_p, want_p) and torch.equal(got_d, want_d)
+
+
+def test_outputs_of_another_stream_may_be_dropped_once_their_use_is_queued():
+    """A result from `stream`, read on the caller's stream: its memory is not given to the next call on
+    `stream` before that."""
+    w, lens = R.G2, [300, 40]
+    c = R.Case(w, lens, 16, 2)
+    cache = PagedCache(w, c.k.cuda(), c.v.cuda(), c.table.cuda())
+    qa, qb = c.queries(2).cuda(), c.queries(2).cuda()
+    ln, cu, pre = i32(lens), i32([0, 1, 2]), None
+    side = torch.cuda.Stream()
+    for call in (lambda q: cache.decode(q, ln, stream=side), lambda q: cache.prefill(q, ln, cu, stream=side)):
+        torch.cuda.synchronize()
+        want = call(qa)
+        torch.cuda.synchronize()
+        kept = want.clone()
+        del want
+        torch.cuda.synchronize()
+        out = call(qa)
+        torch.cuda.current_stream().wait_stream(side)
+        torch.cuda._sleep(100_000_000)
+        used = out.clone()                            # waits on the caller's stream
+        del out
+        later = [call(qb) for _ in range(4)]
+        torch.cuda.synchronize()
+        assert torch.equal(used, kept)
+        del later
+    q1m.check_status()
+
+
 # ---- sums over many keys --------------------------------------------------------------------
 # Values of one sign, so that what an accumulator loses adds up. The bound, relative to the result:
 # a key tile's products are 2 to 16 dependent accumulation steps, each of which cuts at most 2^-23 of
