@@ -305,7 +305,8 @@ q1m_status q1m_attention_recall(const float* lse_sparse, const float* lse_dense,
 /* Synchronizes `stream`, then returns and clears the device-side status latched by the
  * kernels on the current device (Q1M_OK, Q1M_ERR_TIMEOUT, Q1M_ERR_RANGE, Q1M_ERR_PAGE or
  * Q1M_ERR_INVALID from a paged-cache call or, in debug mode, Q1M_ERR_CHECK), or Q1M_ERR_CUDA if
- * the stream reported an error. */
+ * the stream reported an error. A wait that ran out is reported before an older fault, which the
+ * next call then returns. */
 q1m_status q1m_status_poll(void* stream);
 
 /* The message of the last failing call on this thread ("" if none). */
@@ -528,6 +529,11 @@ q1m_status q1m_set_wait_budget(uint64_t cycles);
  * arrives on, with a budget of `cycles`, and returns what q1m_status_poll then reports
  * (Q1M_ERR_TIMEOUT when the wait gave up as designed). The default budget is restored. */
 q1m_status q1m_selftest_wait_timeout(uint64_t cycles, void* stream);
+
+/* The same behind a latched fault (a q1m_status that kernels latch, not Q1M_ERR_TIMEOUT), with
+ * `waits` (1 .. 1000) such waits one after the other: returns Q1M_ERR_TIMEOUT when the first ran
+ * out; the others end at once. The next q1m_status_poll returns `fault`. */
+q1m_status q1m_selftest_timeout_behind(int fault, int waits, uint64_t cycles, void* stream);
 
 #ifdef __cplusplus
 }

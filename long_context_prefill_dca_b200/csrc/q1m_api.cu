@@ -1053,13 +1053,19 @@ int64_t q1m_prefill_bounds(int64_t n, const q1m_params* p, int64_t* ends, int64_
 q1m_status q1m_status_poll(void* stream) {
   cudaError_t e = cudaStreamSynchronize(S(stream));
   if (e != cudaSuccess) return fail(Q1M_ERR_CUDA, "stream error: %s", cudaGetErrorString(e));
-  int st = 0;
-  Q1M_CUDA(cudaMemcpyFromSymbol(&st, g_status, sizeof(int)));
+  DeviceStatus now{};
+  Q1M_CUDA(cudaMemcpyFromSymbol(&now, g_status, sizeof now));
+  const int zero = 0;
+  if (now.timed_out != 0) {        // an older fault is left for the next poll
+    Q1M_CUDA(cudaMemcpyToSymbol(g_status, &zero, sizeof zero, offsetof(DeviceStatus, timed_out)));
+    return fail(Q1M_ERR_TIMEOUT, "a device-side wait ran out");
+  }
+  const int st = now.first;
   if (st != 0) {
-    const int zero = 0, none = -1;
+    const int none = -1;
     int info = -1;
     Q1M_CUDA(cudaMemcpyFromSymbol(&info, g_check_info, sizeof(int)));
-    Q1M_CUDA(cudaMemcpyToSymbol(g_status, &zero, sizeof(int)));
+    Q1M_CUDA(cudaMemcpyToSymbol(g_status, &zero, sizeof zero, offsetof(DeviceStatus, first)));
     Q1M_CUDA(cudaMemcpyToSymbol(g_check_info, &none, sizeof(int)));
     if (st == Q1M_ERR_CHECK) {
       static const char* lists[] = {"", "vertical columns", "slash offsets", "forced diagonals",
@@ -1069,7 +1075,7 @@ q1m_status q1m_status_poll(void* stream) {
     }
     if (st == Q1M_ERR_PAGE) return fail(Q1M_ERR_PAGE, "paged cache: a needed position has no valid page");
     if (st == Q1M_ERR_INVALID) return fail(Q1M_ERR_INVALID, "paged cache: cu_tokens is malformed");
-    return fail((q1m_status)st, st == Q1M_ERR_TIMEOUT ? "a device-side wait ran out" : "device-side range/NaN check failed");
+    return fail((q1m_status)st, "device-side range/NaN check failed");
   }
   return Q1M_OK;
 }
@@ -1146,11 +1152,16 @@ __global__ void selftest_exp2_kernel(const float* x, float* yp, float* ym, float
 }
 
 // one warp waits on a barrier that no thread and no copy ever arrives on
-__global__ void selftest_wait_kernel() {
+// (behind a latched `fault`, 0: none), `waits` times
+__global__ void selftest_wait_kernel(int fault, int waits) {
   __shared__ uint64_t bar;
-  if (threadIdx.x == 0) { mbar_init(&bar, 1); fence_mbar_init(); }
+  if (threadIdx.x == 0) {
+    mbar_init(&bar, 1);
+    fence_mbar_init();
+    if (fault != 0) latch(fault);
+  }
   __syncwarp();
-  mbar_wait(&bar, 0);
+  for (int i = 0; i < waits; ++i) mbar_wait(&bar, 0);
 }
 }  // namespace
 
@@ -1174,16 +1185,28 @@ extern "C" q1m_status q1m_selftest_exp2(const float* x, float* yp, float* ym, fl
   return Q1M_OK;
 }
 
-extern "C" q1m_status q1m_selftest_wait_timeout(uint64_t cycles, void* stream) {
+namespace {
+q1m_status selftest_wait(int fault, int waits, uint64_t cycles, void* stream) {
   Dev dev;
   Q1M_TRY(device_info(&dev));
   Q1M_TRY(q1m_status_poll(stream));
   Q1M_TRY(q1m_set_wait_budget(cycles ? cycles : 1000000ull));
-  selftest_wait_kernel<<<1, 32, 0, S(stream)>>>();
+  selftest_wait_kernel<<<1, 32, 0, S(stream)>>>(fault, waits);
   Q1M_LAUNCHED();
   const q1m_status st = q1m_status_poll(stream);
   Q1M_TRY(q1m_set_wait_budget(0));
   return st;
+}
+}  // namespace
+
+extern "C" q1m_status q1m_selftest_wait_timeout(uint64_t cycles, void* stream) {
+  return selftest_wait(0, 1, cycles, stream);
+}
+
+extern "C" q1m_status q1m_selftest_timeout_behind(int fault, int waits, uint64_t cycles, void* stream) {
+  if (fault > Q1M_ERR_INVALID || fault < Q1M_ERR_PAGE || fault == Q1M_ERR_TIMEOUT || waits < 1 || waits > 1000)
+    return fail(Q1M_ERR_UNSUPPORTED, "fault is not one that kernels latch, or waits not in 1 .. 1000");
+  return selftest_wait(fault, waits, cycles, stream);
 }
 
 // =============================================================================================

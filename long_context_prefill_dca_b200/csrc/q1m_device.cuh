@@ -17,16 +17,21 @@
 namespace q1m {
 
 // ---------------------------------------------------------------------------------------
-// Device status: the first fault a kernel detects is latched here; q1m_status_poll reads
-// and clears it. Waits give up after g_wait_cycles SM clocks (about one second by default).
+// Device status: the first fault a kernel detects is latched here, and in a word of its own
+// whether a wait ran out (an older fault that nobody has polled must neither hide that nor keep
+// it from ending the other waits); q1m_status_poll reads and clears them. Waits give up after
+// g_wait_cycles SM clocks (about one second by default).
 // ---------------------------------------------------------------------------------------
-__device__ int g_status = 0;
+struct DeviceStatus { int timed_out, first; };   // Q1M_ERR_TIMEOUT or 0; the first other fault or 0
+__device__ DeviceStatus g_status = {0, 0};
 __device__ unsigned long long g_wait_cycles = 2000000000ull;
 
-__device__ __forceinline__ void latch(int code) { atomicCAS(&g_status, 0, code); }
+__device__ __forceinline__ void latch(int code) {
+  atomicCAS(code == Q1M_ERR_TIMEOUT ? &g_status.timed_out : &g_status.first, 0, code);
+}
 // A wait that ran out ends the other waits too. Other faults (a value out of range, a missing page)
 // do not: they may be another stream's, and what waits here still arrives.
-__device__ __forceinline__ bool failed() { return *(volatile int*)&g_status == Q1M_ERR_TIMEOUT; }
+__device__ __forceinline__ bool failed() { return *(volatile int*)&g_status.timed_out != 0; }
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));

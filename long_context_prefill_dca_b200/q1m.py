@@ -109,6 +109,7 @@ SIGNATURES = {
     "q1m_profile_read": (c_int, [ctypes.POINTER(c_dbl), ctypes.POINTER(c_i64)]),
     "q1m_launch_count": (c_u64, []),
     "q1m_selftest_wait_timeout": (c_int, [c_u64, c_vp]),
+    "q1m_selftest_timeout_behind": (c_int, [c_int, c_int, c_u64, c_vp]),
     "q1m_selftest_exp2": (c_int, [c_vp, c_vp, c_vp, c_vp, c_i64, c_vp]),
 }
 
@@ -373,6 +374,10 @@ def set_wait_budget(cycles: int) -> None:
 
 def selftest_wait_timeout(cycles: int, stream=None) -> int:
     return library().q1m_selftest_wait_timeout(cycles, stream_handle(stream))
+
+
+def selftest_timeout_behind(fault: int, waits: int, cycles: int, stream=None) -> int:
+    return library().q1m_selftest_timeout_behind(fault, waits, cycles, stream_handle(stream))
 
 
 STAGES = ["table", "keys", "queries", "estimate", "select", "masks", "attn", "merge", "decode"]

@@ -1,5 +1,7 @@
 """What the paged calls promise beside their results: a table's own width, malformed token
 offsets, memory and streams, lengths beyond the table, sums that keep their precision."""
+import time
+
 import numpy as np
 import pytest
 import torch
@@ -271,3 +273,22 @@ def test_shared_prefix_f32_sums_of_the_largest_batch():
         vv = torch.cat([vr, v[shared + b, :, :m].transpose(0, 1)])
         ref, _ = R.attend(w, q[b:b + 1], [lens[b] - 1], kk, vv)
         assert_unbiased(out[b:b + 1], ref)
+
+
+@pytest.mark.parametrize("fault", [-1, -6, -7, -8])
+def test_a_timeout_behind_an_unpolled_fault_is_reported_and_ends_the_other_waits(fault):
+    """20 waits of half a second each that nothing completes, behind a fault that nobody polled: the
+    first runs out, the others end at once, and both codes are reported, one a poll."""
+    q1m.check_status()
+    torch.cuda.synchronize()
+    t0 = time.perf_counter()
+    assert q1m.selftest_timeout_behind(fault, 20, 1_000_000_000) == -5
+    assert time.perf_counter() - t0 < 5
+    assert q1m.status_poll() == fault and q1m.status_poll() == 0
+    c = R.Case(R.G2, [300], 16, 2)
+    cache, q = PagedCache(c.w, c.k.cuda(), c.v.cuda(), c.table.cuda()), c.queries(1)
+    out = cache.decode(q.cuda(), i32([300]))
+    q1m.check_status()
+    ref, _ = R.attend(c.w, q, [299], c.kc[0], c.vc[0])
+    tol, _ = R.bounds(c.w, q, c.kc[0], c.vc[0], False)
+    R.check(c.w, out, None, ref, None, tol, 0, False)

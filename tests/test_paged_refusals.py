@@ -17,3 +17,9 @@ def test_table_width(lib, name):  # noqa: F811
     assert call(lib, name, desc(**wide), **kw) == -2
     assert call(lib, name, desc(table_width=16, **wide), **kw) == -1      # the next check: x
     assert b"too large" not in lib.q1m_last_error()
+
+
+@host_only
+def test_fault_selftest_refusals(lib):  # noqa: F811
+    for fault, waits in ((0, 1), (-5, 1), (-9, 1), (1, 1), (-8, 0), (-8, 1001)):
+        assert lib.q1m_selftest_timeout_behind(fault, waits, 1000, None) == -2
