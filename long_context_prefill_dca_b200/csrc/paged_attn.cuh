@@ -615,7 +615,7 @@ __device__ __forceinline__ PaRow pa_row(const PagedAttnArgs& a, const PaItem& it
   const int ti = R / a.G;
   r.token = it.tok0 + ti;
   r.head = it.g * a.G + (R - ti * a.G);
-  r.p = !r.valid ? -1 : (a.cu ? it.pos0 + ti : min(max(__ldg(a.seq_len + ti), 0), PG_MAX_LEN) - 1);
+  r.p = !r.valid ? -1 : (a.cu ? it.pos0 + ti : min(max(__ldg(a.seq_len + ti), 0), a.c.max_len) - 1);   // as pg_len
   return r;
 }
 

@@ -195,6 +195,23 @@ def test_outputs_of_another_stream_may_be_dropped_once_their_use_is_queued():
     q1m.check_status()
 
 
+def test_shared_prefix_cuts_a_length_beyond_the_table_as_a_whole():
+    """Both parts of a shared-prefix step, the prefix's and the sequence's own, see the same
+    (cut) position when a length is more than its table row holds."""
+    w, page, prefix = R.G2, 16, 512
+    c = R.Case(w, [544, 530], page, 7, prefix=prefix)
+    table = c.table[:, :544 // page].clone()
+    table[(table < 0) | (table >= c.n_pages)] = c.prefix_table[0]
+    cache = PagedCache(w, c.k.cuda(), c.v.cuda(), table.contiguous().cuda(), "f32")
+    q, pre = c.queries(2).cuda(), c.prefix_table.cuda()
+    want = cache.decode_shared(q, i32([544, 530]), pre, prefix)
+    assert q1m.status_poll() == 0
+    for over in (545, 1000, 2 ** 30, 2 ** 31 - 1):
+        got = cache.decode_shared(q, i32([over, 530]), pre, prefix)
+        assert q1m.status_poll() == -8 and q1m.status_poll() == 0
+        assert torch.equal(got, want), over
+
+
 # ---- sums over many keys --------------------------------------------------------------------
 # Values of one sign, so that what an accumulator loses adds up. The bound, relative to the result:
 # a key tile's products are 2 to 16 dependent accumulation steps, each of which cuts at most 2^-23 of
