@@ -397,7 +397,7 @@ typedef struct {
  *    different scratch. Nothing is kept in it between calls.
  *  - Lengths and tables are read on the device when the call runs, so a captured graph may be
  *    replayed with new ones. Runs are bit-identical (sums follow a fixed order).
- *  - batch = 0 or n_tokens = 0 does nothing. */
+ *  - batch = 0 (page_table may be NULL then) or n_tokens = 0 does nothing. */
 
 /* Appends the call's new tokens: k_pages gets fp16(R(pos mod L) k), v_pages fp16(v).
  * cu_tokens NULL: one token per sequence (n_tokens = batch). A token whose position would be

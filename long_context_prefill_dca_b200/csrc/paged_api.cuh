@@ -46,7 +46,7 @@ q1m_status check_cache(const q1m_paged_cache* c, int batch, int hq, const q1m_pa
   q.equal_cost_chunks = 0;
   q.prefill_chunk = 128;           // the paged calls use neither the budgets nor the chunking
   Q1M_TRY(check_shape(1, hq, c->n_kv_heads, c->head_dim, p ? &q : nullptr));
-  if (!c->k_pages || !c->v_pages || !c->page_table || !table) return fail(Q1M_ERR_INVALID, "NULL pointer");
+  if (!c->k_pages || !c->v_pages || (!c->page_table && batch > 0) || !table) return fail(Q1M_ERR_INVALID, "NULL pointer");
   if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
     return fail(Q1M_ERR_UNSUPPORTED, "page_size %d (16, 32, 64 or 128 supported)", c->page_size);
   if (c->n_pages <= 0 || c->table_stride <= 0) return fail(Q1M_ERR_INVALID, "n_pages and table_stride must be positive");

@@ -292,6 +292,21 @@ def test_shared_prefix_f32_sums_of_the_largest_batch():
         assert_unbiased(out[b:b + 1], ref)
 
 
+def test_an_empty_table_serves_an_empty_batch():
+    w = R.G2
+    c = R.Case(w, [40], 16)
+    cache = PagedCache(w, c.k.cuda(), c.v.cuda(), c.table.cuda()[:0], "bf16")
+    z = torch.empty(0, w.n_kv_heads, w.head_dim, dtype=torch.bfloat16, device="cuda")
+    zq = torch.empty(0, w.n_q_heads, w.head_dim, dtype=torch.bfloat16, device="cuda")
+    none, before = torch.empty(0, dtype=torch.int32, device="cuda"), q1m.launch_count()
+    cache.append(z, z, none)
+    cache.append(z, z, none, i32([0]))
+    assert cache.decode(zq, none).shape == (0, 4, 128)
+    assert cache.decode_shared(zq, none, i32([0] * 8), 128).shape[0] == 0
+    assert cache.prefill(zq, none, i32([0])).shape[0] == 0
+    assert q1m.launch_count() == before
+
+
 @pytest.mark.parametrize("fault", [-1, -6, -7, -8])
 def test_a_timeout_behind_an_unpolled_fault_is_reported_and_ends_the_other_waits(fault):
     """20 waits of half a second each that nothing completes, behind a fault that nobody polled: the

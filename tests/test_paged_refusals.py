@@ -1,5 +1,5 @@
 """Refusals and empty calls of the paged cache on the host, before anything touches a GPU (CPU
-only): the width of a table row."""
+only): the width of a table row, an empty batch, the self-test of the status words."""
 import pytest
 
 from tests.test_paged_abi import CALLS, call, desc, host_only, lib  # noqa: F401  (lib: a fixture)
@@ -23,3 +23,10 @@ def test_table_width(lib, name):  # noqa: F811
 def test_fault_selftest_refusals(lib):  # noqa: F811
     for fault, waits in ((0, 1), (-5, 1), (-9, 1), (1, 1), (-8, 0), (-8, 1001)):
         assert lib.q1m_selftest_timeout_behind(fault, waits, 1000, None) == -2
+
+
+@host_only
+@pytest.mark.parametrize("name", CALLS)
+def test_an_empty_batch_needs_no_table(lib, name):  # noqa: F811
+    assert call(lib, name, desc(page_table=None), batch=0, n=0) == 0
+    assert call(lib, name, desc(page_table=None)) == -1
