@@ -765,6 +765,11 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
     bool ok = true;
     uint32_t e = 0, joins = 0;
     for (; p.o < n_mine; p.next(a, n_mine)) {
+      // which CTAs have parts of the pair: before any wait, so that the merge finds it in any case
+      if (a.pairs && threadIdx.x == 0 && p.i0 == 0) {
+        const int n_own = p.take == p.s.n ? 1 : R.owner(first_unit(p) + p.s.n - 1) - (int)blockIdx.x + 1;
+        a.pairs[(int64_t)p.b * hkv + p.g] = make_int2((int)blockIdx.x, n_own);
+      }
       float m_run = -INFINITY, l_run = 0.f;
       float oacc[DN][2];
 #pragma unroll
@@ -899,13 +904,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
       arrived = __shfl_sync(0xFFFFFFFFu, arrived, 0);
       if (arrived == n_parts - 1) {
         __threadfence_block();
-        if (lane == 0) {
-          sm.joined[p.k % PD_JOINS] = 0;
-          if (a.pairs && p.i0 == 0) {
-            const int n_own = p.take == p.s.n ? 1 : R.owner(first_unit(p) + p.s.n - 1) - (int)blockIdx.x + 1;
-            a.pairs[(int64_t)p.b * hkv + p.g] = make_int2((int)blockIdx.x, n_own);
-          }
-        }
+        if (lane == 0) sm.joined[p.k % PD_JOINS] = 0;
         if (ok) pd_join<TO, D>(sm, a, p, n_parts);
         __syncwarp();
         if (lane < n_parts) mbar_arrive(&sm.o_free[(p.o + lane) & (PD_WARPS - 1)]);
