@@ -22,11 +22,10 @@ constexpr int32_t PG_MAX_LEN = 1 << 30;   // positions of a sequence
 struct PagedCacheArgs {
   const int32_t* page_table;   // [batch] rows
   int64_t table_stride;        // entries between rows
-  int64_t table_width;         // entries of a row: those behind it are not the cache's
   int32_t n_pages;
   int32_t page_log2;           // page_size = 1 << page_log2, 16 .. 128
   int32_t hkv;
-  int32_t max_len;             // positions that a table row can hold, PG_MAX_LEN at most
+  int32_t max_len;             // positions that a table row's own entries hold, PG_MAX_LEN at most
 };
 
 // dca_query_pos in 32 bits (a 64-bit remainder takes over 100 cycles more).
@@ -67,7 +66,7 @@ __device__ __forceinline__ bool pg_wait(uint64_t* bar, uint32_t parity, volatile
 // Page of entry `i` of a table row, -1 when the row has no such entry or the entry is not a page of
 // the cache.
 __device__ __forceinline__ int32_t pg_entry(const PagedCacheArgs& c, const int32_t* row, int64_t i) {
-  if (i >= c.table_width) return -1;
+  if (i >= c.max_len >> c.page_log2) return -1;
   const int32_t page = __ldg(row + i);
   return page < c.n_pages ? page : -1;
 }

@@ -90,11 +90,10 @@ PagedCacheArgs cache_args(const q1m_paged_cache* c) {
   PagedCacheArgs a{};
   a.page_table = c->page_table;
   a.table_stride = c->table_stride;
-  a.table_width = table_width(c);
   a.n_pages = (int32_t)c->n_pages;
   a.page_log2 = c->page_size == 16 ? 4 : c->page_size == 32 ? 5 : c->page_size == 64 ? 6 : 7;
   a.hkv = c->n_kv_heads;
-  const int64_t held = a.table_width < PG_MAX_LEN ? a.table_width * c->page_size : PG_MAX_LEN;
+  const int64_t width = table_width(c), held = width < PG_MAX_LEN ? width * c->page_size : PG_MAX_LEN;
   a.max_len = (int32_t)(held < PG_MAX_LEN ? held : PG_MAX_LEN);
   return a;
 }
@@ -252,7 +251,7 @@ q1m_status paged_decode(const void* q, int64_t q_stride, const int32_t* seq_len,
     PagedAttnArgs t{};
     t.c = a.c;
     t.c.page_table = prefix_table;
-    t.c.table_stride = t.c.table_width = prefix_len / c->page_size;
+    t.c.table_stride = prefix_len / c->page_size;
     t.q = q; t.q_stride = q_stride; t.n_tokens = batch;
     t.q_f32 = p->in_dtype == Q1M_F32;
     t.seq_len = seq_len;

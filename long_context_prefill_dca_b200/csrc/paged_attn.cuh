@@ -394,7 +394,7 @@ __device__ void pa_loader(PaSmem<D>& sm, const PagedAttnArgs& a, const CUtensorM
     };
     auto entry = [&](int key0) {
       const int i = (key0 >> lp) + pg;
-      return needed(key0) && i < a.c.table_width ? __ldg(row + i) : -1;
+      return needed(key0) ? __ldg(row + i) : -1;       // a visible key lies within the table (pg_len)
     };
     int32_t page = entry(it.tile(0) * 128);
     for (int i = 0; i < it.take; ++i, ++kt) {
