@@ -63,6 +63,19 @@ __device__ __forceinline__ bool pg_wait(uint64_t* bar, uint32_t parity, volatile
   return __all_sync(0xFFFFFFFFu, ok);
 }
 
+// Wait of one thread for what the hardware has under way (a copy, an MMA) and ends by itself. Its
+// limit is its own: neither a short wait budget nor another warp's giving up may let a CTA end, or
+// free its tensor memory, before.
+__device__ __forceinline__ void pg_land(uint64_t* bar, uint32_t parity) {
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity)) {
+    if (clock64() - t0 > 2000000000ll) {
+      latch(Q1M_ERR_TIMEOUT);
+      break;
+    }
+  }
+}
+
 // Page of entry `i` of a table row, -1 when the row has no such entry or the entry is not a page of
 // the cache.
 __device__ __forceinline__ int32_t pg_entry(const PagedCacheArgs& c, const int32_t* row, int64_t i) {
@@ -692,6 +705,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
     int cur[2], nxt[2];
     lookup(lane, nxt);
     bool ok = true;
+    int issued = 0;
     for (int o0 = 0; o0 < n_mine && ok; o0 += 32) {
       cur[0] = nxt[0]; cur[1] = nxt[1];
       const int n = min(32, n_mine - o0);
@@ -709,11 +723,13 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
           if (lp == 4) tma_load_3d(sm.v[st] + PdSmem<D>::TILE / 2, &mv, full, 0, cur[1], 0);
         }
         __syncwarp();
+        issued = o + 1;
       }
     }
-    if (!ok) {   // let copies already issued land before the CTA's memory goes
-      const long long t0 = clock64();
-      while (clock64() - t0 < 2000000) __nanosleep(1000);
+    // whoever gave up, the last copies land before the CTA's memory goes
+    if (lane < min(issued, PD_STAGES)) {
+      const uint32_t o = issued - 1 - lane, turn = o / PD_STAGES;
+      pg_land(&sm.full[o % PD_STAGES][turn & 1], (turn >> 1) & 1);
     }
   } else if (w > PD_WARPS) {
     // ---- query views: every PD_QUERY_WARPS-th of the run's (piece, view) list, the loads of

@@ -351,7 +351,7 @@ struct PaSmem {
   PaWalk walk[10];                          // and the one before or behind it
   PaPlan plan;
   uint32_t tmem_base;
-  int gave_up, never;                       // never: 0, for a wait that no other warp cuts short
+  int gave_up;
 };
 
 // ---------------------------------------------------------------------------------------
@@ -436,10 +436,8 @@ __device__ void pa_loader(PaSmem<D>& sm, const PagedAttnArgs& a, const CUtensorM
       page = page_next;
     }
   }
-  if (!ok) {   // let copies already issued land before the CTA's memory goes
-    const long long t0 = clock64();
-    while (clock64() - t0 < 2000000) __nanosleep(1000);
-  }
+  // whoever gave up, the last copies land before the CTA's memory goes (kt: tiles issued)
+  if (lane < min((int)kt, NS)) pg_land(&full[(kt - 1 - lane) % NS], ((kt - 1 - lane) / NS) & 1);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -595,7 +593,7 @@ __device__ void pa_mma(PaSmem<D>& sm, const PagedAttnArgs& a) {
   // whatever else went wrong, the MMAs already issued end before tensor memory is freed
   if (elect_one()) mma_commit(&sm.drain);
   __syncwarp();
-  pg_wait(&sm.drain, 0, &sm.never);
+  pg_land(&sm.drain, 0);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -977,7 +975,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
     }
     mbar_init(&sm.drain, 1);
     fence_mbar_init();
-    sm.gave_up = sm.never = 0;
+    sm.gave_up = 0;
   }
   if (w == 9) { tmem_alloc(&sm.tmem_base, 512); tmem_relinquish(); }
   if (w == 8 && lane_id() == 0) { tma_prefetch(&mk); tma_prefetch(&mv); }
