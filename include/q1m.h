@@ -364,7 +364,11 @@ q1m_status q1m_dca_decode(const void* q, const void* k, const void* v, int64_t p
  *    [0, n_pages) latches Q1M_ERR_PAGE; the append then skips that token and the attention
  *    reads zeros for the page.
  *  - page_size: 16, 32, 64 or 128 tokens. A sequence has at most 2^30 positions.
- * Rows behind a sequence's last position are never used, whatever they hold (NaN included). */
+ * Rows behind a sequence's last position are never used, whatever they hold (NaN included). The
+ * keys and values of its positions are finite (the append reports others): a NaN or infinity in a
+ * key reaches the queries that see it; one in a value may also reach queries of its KV head that do
+ * not (a weight of 0 times NaN): in a prefill those of the same sequence, in a shared prefix those
+ * of sequences that are shorter than the prefix. */
 typedef struct {
   uint16_t* k_pages;
   uint16_t* v_pages;
