@@ -54,7 +54,7 @@ __device__ __forceinline__ bool pg_wait(uint64_t* bar, uint32_t parity, volatile
       if (mbar_try_wait(bar, parity)) { ok = true; break; }
       if (*gave_up) break;
       if ((unsigned long long)(clock64() - t0) > budget) {
-        latch(Q1M_ERR_TIMEOUT);
+        latch_timeout();
         *gave_up = 1;
         break;
       }
@@ -70,7 +70,7 @@ __device__ __forceinline__ void pg_land(uint64_t* bar, uint32_t parity) {
   const long long t0 = clock64();
   while (!mbar_try_wait(bar, parity)) {
     if (clock64() - t0 > 2000000000ll) {
-      latch(Q1M_ERR_TIMEOUT);
+      latch_timeout();
       break;
     }
   }
