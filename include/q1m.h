@@ -396,6 +396,12 @@ typedef struct {
  *    keys (i - window < j <= i) and the first `sinks` ones (j < sinks, j <= i).
  *  - out [rows][n_q_heads][head_dim] in p->out_dtype, contiguous, 16-byte aligned; lse
  *    (nullable) [n_q_heads][rows] fp32, natural log. A row that sees no key gets zeros and -inf.
+ *  - out_dtype also chooses the precision inside q1m_paged_prefill and of the prefix's part of
+ *    q1m_shared_prefix_decode. Q1M_F32: rotated queries and softmax weights enter the products as
+ *    two fp16 numbers each (22 bits), results are within about 1e-6 of 64 bits. Q1M_BF16: as one
+ *    (11 bits, as in the contiguous prefill), which together with the result's own rounding gives
+ *    1.7e-3 rms where rounding alone gives 1.66e-3, at half the tensor work. q1m_paged_decode takes
+ *    two either way, so bf16 results of the two decodes of one batch differ by about 1e-3.
  *  - Of p the DCA, YaRN and dtype fields are used; table as for q1m_dca_decode.
  *  - scratch: the call's own, 256-byte aligned; calls that may overlap on the GPU need
  *    different scratch. Nothing is kept in it between calls.
@@ -427,8 +433,8 @@ size_t q1m_shared_prefix_decode_scratch_bytes(int batch, int64_t prefix_len, int
 
 /* q1m_paged_decode (all keys) for sequences whose first prefix_len positions are the same
  * pages, prefix_table[0 .. prefix_len / page_size) (device int32), all of them in the cache: the
- * prefix is read once for the whole batch, on the tensor cores. prefix_len is a multiple of page_size and at least 128;
- * the part behind its last multiple of 128 and everything after it is read through page_table
+ * prefix is read once for the whole batch, on the tensor cores. prefix_len is a multiple of
+ * page_size and at least 128; the part behind its last multiple of 128 and everything after it is read through page_table
  * (whose rows count from position 0; their earlier entries are not read). Sequences shorter
  * than the prefix see their own part of it. */
 q1m_status q1m_shared_prefix_decode(const void* q, int64_t q_stride, const int32_t* seq_len,

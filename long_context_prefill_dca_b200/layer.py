@@ -162,6 +162,8 @@ class PagedCache:
     page_table: int32 [batch, pages], a slice of a larger table if need be: position j of sequence
     b is row j % page_size of page page_table[b, j // page_size]. Only entries of pages a call
     needs are read.
+    out_dtype: "f32" (results within about 1e-6 of 64 bits; the prefill and the shared prefix take
+    twice the tensor work) or "bf16" (their queries and weights are rounded to fp16).
     table: the RoPE table [dca_chunk, D / 2, 2] when the caller has one already; otherwise the
     constructor computes it and waits until it is there.
 
