@@ -306,15 +306,16 @@ paged_append_kernel(const PagedAppendArgs a, int units, int tokens) {
 //  * Each tile's product P V is a fresh sum that is added to the warp's total with rounding: the
 //    tensor core cuts what it adds to an accumulator towards zero, so a total kept in its
 //    accumulator lost 1.0e-4 of the result at 131,000 keys a pair and 1.2e-5 at 16,000 (values of
-//    one sign); this way 9e-8, and no slower (128 windowed sequences 120 us, 123 before).
+//    one sign); this way 9e-8, and no slower (128 windowed sequences 119 us, 123 before: half the
+//    accumulators, as hi and lo rows are added tile by tile, and no spills).
 //  * Rows of a tile that the token does not see (past its end, between sinks and window) are
 //    masked in S and zeroed in the V tile: whatever an unwritten page holds meets no product.
 //    Pages that hold no visible key are not looked up; TMA fills their rows with zeros.
 //
-// Measured with the merge, from a captured graph: 131,071 keys of 4 KV heads, D = 128 (268 MB) 55
-// us; 1,048,575 keys (2.1 GB) 315 us in pages of 128 (6.8 TB/s) and 343 us in pages of 16 (6.3);
-// 128 sequences with 4,096-key windows (670 MB) 124 us, 5.4 TB/s; 48 of 1 .. 32,768 keys (590 MB,
-// pages of 16) 121 us. About 3 us pass until a CTA knows its run, 2 more until its first tile
+// Measured with the merge, from a captured graph: 131,071 keys of 4 KV heads, D = 128 (268 MB) 54
+// us; 1,048,575 keys (2.1 GB) 314 us in pages of 128 (6.9 TB/s) and 341 us in pages of 16 (6.3);
+// 128 sequences with 4,096-key windows (670 MB) 120 us, 5.6 TB/s; 48 of 1 .. 32,768 keys (590 MB,
+// pages of 16) 116 to 119 us on different boxes. About 3 us pass until a CTA knows its run, 2 more until its first tile
 // has landed, and 5 go to the merge.
 // ---------------------------------------------------------------------------------------
 constexpr int PD_WARPS = 8;                 // consumer warps
@@ -326,8 +327,9 @@ constexpr int PD_QUERIES = 4;               // query views in flight
 constexpr int PD_JOINS = 32;                // pairs in flight at most: warps are within 18 tiles of
                                             // one another (each takes every eighth, 10 stages)
 // of a (sequence, KV head) pair, in tiles: short pairs that many warps take at once cost about 4,
-// ones of a dozen tiles about 9 (128 windowed sequences: 129 us at 6, 120 at 9; 48 sequences of
-// 1 .. 32,768 keys: 112 us at 4, 117 at 9)
+// ones of a dozen tiles about 9; one value for both, so that mixed batches of many short sequences
+// pay for the others (128 windowed sequences: 134, 124, 119 and 119 us at 4, 6, 8 and 9; 48
+// sequences of 1 .. 32,768 keys: 110, 113, 118 and 116)
 constexpr int PD_PAIR_COST = 8;
 constexpr int PD_MIN_UNITS = PD_PAIR_COST + 4;   // of a CTA's run at least
 // weights are kept as 2^PD_BIAS p in fp16 (p <= 1), so that its subnormals start at 2^-26

@@ -32,9 +32,11 @@
 //    buffer holds the low parts, P's low parts follow the high ones in S's columns), twice the
 //    MMAs on one slot, whose products are summed tile by tile: 3e-7 to 6e-7 off 64 bits.
 //
-// Measured (captured graph, G = 7, D = 128, bf16): 1,000 tokens over 32,700 keys 457 us, 1.01
-// PFLOP/s; 16,384 tokens with a 4,096-key window 1,089 us, 0.90; 8 sequences behind 262,144
-// shared keys (537 MB) 100 us, 5.4 TB/s.
+// Measured (captured graph, G = 7, D = 128, bf16): 1,000 tokens over 32,700 keys 443 us, 1.04
+// PFLOP/s; 16,384 tokens with a 4,096-key window 1,084 us, 0.90; with 32-bit outputs 1,113 and 2,752
+// us. Behind 262,144 shared keys (537 MB) 8 sequences take this kernel 100 us, 5.4 TB/s, and the
+// call, with their own keys (22 us) and the merge (6 us) around it, 120 to 126; with 32-bit outputs
+// the call takes 200.
 #pragma once
 
 #include "paged.cuh"
