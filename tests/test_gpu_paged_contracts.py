@@ -324,3 +324,20 @@ def test_a_timeout_behind_an_unpolled_fault_is_reported_and_ends_the_other_waits
     ref, _ = R.attend(c.w, q, [299], c.kc[0], c.vc[0])
     tol, _ = R.bounds(c.w, q, c.kc[0], c.vc[0], False)
     R.check(c.w, out, None, ref, None, tol, 0, False)
+
+
+@pytest.mark.parametrize("out_dtype", ["f32", "bf16"])
+def test_shared_prefix_behind_a_table_narrower_than_it(out_dtype):
+    """Sequences that end inside the prefix need no table entries for the rest of it."""
+    w, page, prefix, lens = R.G2, 16, 512, [150, 100, 1]
+    c = R.Case(w, lens, page, 9, prefix=prefix)
+    narrow = torch.full((3, 10), -1, dtype=torch.int32, device="cuda")
+    cache = PagedCache(w, c.k.cuda(), c.v.cuda(), narrow, out_dtype)
+    q = c.queries(3)
+    out = cache.decode_shared(q.cuda(), i32(lens), c.prefix_table.cuda(), prefix)
+    torch.cuda.synchronize()
+    q1m.check_status()
+    for b, ln in enumerate(lens):
+        ref, _ = R.attend(w, q[b:b + 1], [ln - 1], c.kc[b], c.vc[b])
+        tol, _ = R.bounds(w, q[b:b + 1], c.kc[b], c.vc[b], out_dtype == "bf16")
+        R.check(w, out[b:b + 1], None, ref, None, tol, 0, out_dtype == "bf16")
