@@ -341,3 +341,29 @@ def test_shared_prefix_behind_a_table_narrower_than_it(out_dtype):
         ref, _ = R.attend(w, q[b:b + 1], [ln - 1], c.kc[b], c.vc[b])
         tol, _ = R.bounds(w, q[b:b + 1], c.kc[b], c.vc[b], out_dtype == "bf16")
         R.check(w, out[b:b + 1], None, ref, None, tol, 0, out_dtype == "bf16")
+
+
+@pytest.mark.parametrize("out_dtype", ["f32", "bf16"])
+def test_waits_that_run_out_at_once_leave_nothing_behind(out_dtype):
+    """A wait budget of one cycle: calls may give up (the status says so) at any of their waits; no
+    copy or MMA outlives its CTA, nothing unset is used as an address, and with the default budget
+    the same buffers give the results that they gave before."""
+    w, lens, prefix = R.G2, [5000, 700, 1300, 0], 384
+    c = R.Case(w, lens, 32, 5, prefix=prefix)
+    cache, ln, pre, new = PagedCache(w, c.k.cuda(), c.v.cuda(), c.table.cuda(), out_dtype), i32(lens), c.prefix_table.cuda(), 600
+    q, qp, cu = c.queries(4).cuda(), c.queries(2 * new + 100).cuda(), i32([0, new, 2 * new, 2 * new + 100, 2 * new + 100])
+    calls = [lambda: cache.decode(q, ln), lambda: cache.decode(q, ln, 300, 7), lambda: cache.decode_shared(q, ln, pre, prefix),
+             lambda: cache.prefill(qp, ln, cu), lambda: cache.prefill(qp, ln, cu, 200, 5)]
+    want = [f() for f in calls]
+    q1m.check_status()
+    try:
+        q1m.set_wait_budget(1)
+        for f in calls:
+            f()
+            assert q1m.status_poll() in (0, -5)
+    finally:
+        q1m.set_wait_budget(0)
+    assert q1m.status_poll() == 0
+    for f, x in zip(calls, want):
+        assert torch.equal(f(), x)
+    q1m.check_status()
